@@ -236,7 +236,9 @@ __global__ void __launch_bounds__(kBwdThreads, kBwdBlocks) rope_bwd_kernel(const
       Eight f = fma8(unpack8(partners<kInter, kC>(rg[i], a)), a.s, mul8(unpack8(rg[i]), a.c));
       if (kNorm) {
         const Eight v = unpack8(rx[i]), fv = mul8(f, v);
-        const float r = rsqrtf(group_sum<kC>(dot8(v, v)) * (1.0f / D) + p.eps);
+        // rows that are not there or are left out: r of zeros would be infinite for eps = 0, and dw NaN
+        const float ms = group_sum<kC>(dot8(v, v)) * (1.0f / D) + p.eps;
+        const float r = row && h0 + i * kG < S.H ? rsqrtf(ms) : 0.0f;
         const float c = group_sum<kC>(dot8(fv, w)) * (1.0f / D) * r * r;  // mean(g' w xh) r
         const uint64_t r2 = pack2(r, r), m2 = pack2(-c * r, -c * r);
         dw = fma8(fv, Eight{{r2, r2, r2, r2}}, dw);

@@ -13,6 +13,8 @@
  *   dx = r * (g' w - xh * mean(g' w xh)),  xh = x r;  dw = sum over rows of g' xh
  *   dx = g'                                                (norm = 0)
  * All arithmetic is FP32 on bf16 inputs, rounded once to bf16; dw stays FP32.
+ * (So mean(x^2) has to be an FP32 number, and not 0 where eps = 0: a row of zeros,
+ * or of magnitudes below 2^-70, then has no norm and gives NaN or infinity.)
  *
  * The library takes cos and sin from the caller's table, cos_sin[max_pos][rot]
  * (FP32, cos of pair i at i, sin at rot/2 + i), so that a table made in 64 bits

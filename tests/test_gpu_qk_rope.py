@@ -333,3 +333,34 @@ def test_the_rotation_in_front_of_sagebwd_trains():
     # the same gradients as through the two backward calls by hand
     o2 = SB.attention(*y2, v.detach(), causal=True)
     assert torch.equal(o2, o)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hk", [(12, 4), (8, 8), (9, 1), (32, 16)])
+@pytest.mark.parametrize("inter", [False, True])
+def test_an_eps_of_zero_and_heads_that_leave_a_rest(D, Hq, Hk, inter):
+    # heads that do not fill a warp's unit, and a token left out whose rows are zeros
+    B, N, rot = 2, 21, 48
+    rng, q, k, w = case(15, B, N, Hq, Hk, D)
+    q[1, 3], k[1, 3] = 0.0, 0.0
+    pos = rng.integers(0, 500, (B, N))
+    pos[1, 3] = 500
+    live = (pos < 500).reshape(-1)
+    table = Q.rope_table(500, rot)
+    p = torch.from_numpy(pos.astype(np.int32)).cuda()
+    gq, gk = (bf16(0.01 * rng.standard_normal((B, N, h, D))) for h in (Hq, Hk))
+    y = Q.forward(q, k, p, table, *w, eps=0.0, interleaved=inter)
+    back = Q.backward(gq, gk, q, k, p, table, *w, eps=0.0, interleaved=inter)
+    assert table.get_status() == S.EINDEX
+    cos, sin = (x.reshape(B * N, -1)[live] for x in R.rope_angles(pos, rot))
+    for x, wx, got, g, dx, dw in ((q, w[0], y[0], gq, back[0], back[2]), (k, w[1], y[1], gk, back[1], back[3])):
+        x, g = (R.f64(t).reshape(B * N, -1, D)[live] for t in (x, g))
+        rms, wx = np.sqrt((x * x).mean(-1, keepdims=True)), R.f64(wx)
+        ry, (rdx, rdw) = R.rope(x, cos, sin, rot, inter, wx, 0.0), R.rope_back(x, g, cos, sin, rot, inter, wx, 0.0)
+        got, dx = (t.reshape(B * N, -1, D) for t in (got, dx))
+        on = torch.from_numpy(live)
+        close(got.cpu()[on], ry, np.abs(ry).max(-1, keepdims=True) * 2, "y")
+        close(dx.cpu()[on], rdx, np.abs(wx).max() / rms * np.abs(g).max(-1, keepdims=True) * 8, "dx")
+        assert (got.cpu()[~on] == 0).all() and (dx.cpu()[~on] == 0).all()
+        a = np.abs(g).max() * 1.5 * np.abs(x / rms).reshape(-1, D).sum(0)
+        assert (np.abs(R.f64(dw) - rdw) <= a * (2.0 ** -20 + 2.0 ** -24 * (x.shape[0] * x.shape[1]) ** 0.5 + 2.0 ** -20)).all()
