@@ -342,14 +342,23 @@ def _autograd_function():
 _fn = None
 
 
+def _tangents(*tensors) -> bool:
+    """Whether one of them has a forward-mode tangent (which the autograd function refuses)."""
+    from torch.autograd import forward_ad
+    if forward_ad._current_level < 0:  # as nearly always: no call for each tensor
+        return False
+    return any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+
+
 def norm_rope(q, k, positions, table: RopeTable, q_weight=None, k_weight=None, eps: float = 1e-6,
               interleaved: bool = False, layout: str = "NHD", out_layout: str | None = None):
     """Norms and rotation of q and k (see ``forward``), differentiable in q, k
-    and the norms' weights."""
+    and the norms' weights (backward only: forward-mode tangents are refused)."""
     import torch
     global _fn
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or (
-            q_weight is not None and q_weight.requires_grad) or (k_weight is not None and k_weight.requires_grad)):
+            q_weight is not None and q_weight.requires_grad) or (k_weight is not None and k_weight.requires_grad)) or \
+            _tangents(q, k, q_weight, k_weight):
         if _fn is None:
             _fn = _autograd_function()
         return _fn.apply(q, k, positions, q_weight, k_weight, table, eps, interleaved, layout, out_layout)

@@ -364,3 +364,23 @@ def test_an_eps_of_zero_and_heads_that_leave_a_rest(D, Hq, Hk, inter):
         assert (got.cpu()[~on] == 0).all() and (dx.cpu()[~on] == 0).all()
         a = np.abs(g).max() * 1.5 * np.abs(x / rms).reshape(-1, D).sum(0)
         assert (np.abs(R.f64(dw) - rdw) <= a * (2.0 ** -20 + 2.0 ** -24 * (x.shape[0] * x.shape[1]) ** 0.5 + 2.0 ** -20)).all()
+
+
+def test_forward_mode_is_refused():
+    import torch.autograd.forward_ad as F
+    rng, q, k, w = case(16, 1, 6, 2, 2, 64)
+    table = Q.rope_table(8, 64)
+    p = torch.arange(6, dtype=torch.int32, device="cuda")
+    ref = Q.norm_rope(q, k, p, table, *w)
+    with F.dual_level():  # no input has a tangent
+        assert all(torch.equal(a, b) for a, b in zip(Q.norm_rope(q, k, p, table, *w), ref))
+    for i in range(4):
+        with F.dual_level():
+            x = [q, k, *w]
+            x[i] = F.make_dual(x[i], torch.ones_like(x[i]))
+            with pytest.raises(NotImplementedError):
+                Q.norm_rope(x[0], x[1], p, table, x[2], x[3])
+            with torch.no_grad(), pytest.raises(NotImplementedError):
+                Q.norm_rope(x[0], x[1], p, table, x[2], x[3])
+    with pytest.raises(RuntimeError):
+        torch.func.jvp(lambda x: Q.norm_rope(x, k, p, table, *w)[0], (q.contiguous(),), (torch.ones_like(q),))
