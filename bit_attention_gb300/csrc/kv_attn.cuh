@@ -69,7 +69,8 @@ __device__ __forceinline__ long long share_of(long long units, int workers, long
 __device__ __forceinline__ int2 key_range(const AttnArgs& a, int len, int nq, int i) {
   const int pos = len - nq + i;
   const int hi = a.causal ? min(len, pos + 1) : len;
-  const int lo = a.window ? max(0, pos - a.window + 1) : 0;
+  // (pos may be negative and the window any int: no difference of the two below 0)
+  const int lo = a.window && pos >= a.window ? pos - a.window + 1 : 0;
   return int2{lo, hi};
 }
 

@@ -606,3 +606,16 @@ def test_offsets_beyond_32_bits():
         KV.append(small, kv[:, :H], kv[:, H:], cu, n, t2)
         assert torch.equal(o, KV.attention(q, small, cu, n, t2))
     assert c.get_status() == S.OK
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("q_lens,kv_lens,G", [([5, 1], [2, 40], 2), ([150, 3], [70, 2], 4)])
+def test_the_widest_windows_and_tokens_before_the_first_position(fmt, q_lens, kv_lens, G):
+    # more new tokens than the cache holds: their windows begin before any int32
+    b = R.Batch(fmt, 2, 64, 16, q_lens, kv_lens, seed=29)
+    q = bf16(b.rng.standard_normal((b.T, 2 * G, 64)))
+    for window in (2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 60, 30):
+        for causal in (True, False):
+            o, lse = KV.attention(q, b.cache, *b.args(), causal=causal, window=window, return_lse=True)
+            R.check_attention(b, q, o, lse, causal=causal, window=window, label=f"{window} {causal}")
+    assert b.cache.get_status() == S.OK
