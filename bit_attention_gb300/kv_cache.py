@@ -23,6 +23,7 @@ from . import sage_fp4 as _fp4
 from .sage_fp4 import EINVAL, SageFp4Error, sage_fp4_strides
 
 _HEADER = os.path.join(os.path.dirname(_fp4._HEADER), "sage_kv.h")
+INT32_MAX = 0x7fffffff
 FORMATS = {"bf16": 0, "e4m3": 1, "nvfp4": 2}  # SAGE_KV_*
 _lock = threading.Lock()
 _declared = set()
@@ -187,8 +188,8 @@ def _batch(cache: PagedCache, cu_q, kv_len, block_table) -> sage_kv_batch:
             raise SageFp4Error(EINVAL, f"{nm} must be an int32 tensor on the cache's device")
     if B < 0 or not kv_len.is_contiguous() or (cu_q is not None and (cu_q.shape != (B + 1,) or not cu_q.is_contiguous())):
         raise SageFp4Error(EINVAL, "kv_len must be a contiguous [B], cu_q a contiguous [B + 1] tensor")
-    if len(ts) != 2 or ts[0] != B:
-        raise SageFp4Error(EINVAL, f"block_table must be [{B}, pages]")
+    if len(ts) != 2 or ts[0] != B or max(B, ts[1]) > INT32_MAX:
+        raise SageFp4Error(EINVAL, f"block_table must be [{B}, pages], both below 2^31")
     pages, (row, one) = ts[1], block_table.stride()
     if (pages > 1 and one != 1) or (B > 1 and row < pages):
         raise SageFp4Error(EINVAL, "block_table must have a contiguous last axis and rows of their own")
@@ -205,6 +206,8 @@ def _rows(x, cache: PagedCache, name: str, H: int | None = None):
         raise SageFp4Error(EINVAL, f"{name} must be a bf16 tensor [T, heads, {cache.D}] on the cache's device with a "
                                    "contiguous last axis")
     t, h, _ = shape
+    if max(t, h) > INT32_MAX:  # a broadcast tensor; ctypes would cut the numbers
+        raise SageFp4Error(EINVAL, f"{name} has {t} rows of {h} heads, more than 2^31 - 1")
     if H is not None and h != H:
         raise SageFp4Error(EINVAL, f"{name} has {h} heads, not {H}")
     return t, h, sage_kv_rows(stride[0] if t > 1 else 0, stride[1] if h > 1 else 0)
@@ -229,7 +232,7 @@ def read(cache: PagedCache, kv_len, block_table, N: int, layout: str = "HND", ou
     length are zeros.  out: (k, v) to write instead of new tensors."""
     import torch
     batch = _batch(cache, None, kv_len, block_table)
-    if layout not in _fp4.LAYOUTS or N < 0:
+    if layout not in _fp4.LAYOUTS or not 0 <= N <= INT32_MAX:
         raise SageFp4Error(EINVAL, f"layout must be one of {_fp4.LAYOUTS}, not {layout!r}; N = {N}")
     B, H, D = batch.B, cache.H, cache.D
     shape = (B, H, N, D) if layout == "HND" else (B, N, H, D)
@@ -285,8 +288,8 @@ def attention(q, cache: PagedCache, cu_q, kv_len, block_table, causal: bool = Tr
     T, Hq, qr = _rows(q, cache, "q")
     if Hq < 1 or Hq % cache.H:
         raise SageFp4Error(EINVAL, f"{Hq} query heads over {cache.H} key/value heads")
-    if window is not None and not 1 <= window <= 0x7fffffff:
-        raise SageFp4Error(EINVAL, f"window must be at least 1, not {window}")
+    if window is not None and not 1 <= window <= INT32_MAX:
+        raise SageFp4Error(EINVAL, f"window must be from 1 to 2^31 - 1, not {window}")
     if out is None:
         out = torch.empty((T, Hq, cache.D), dtype=torch.bfloat16, device=cache.device)
         orow = sage_kv_rows(Hq * cache.D, cache.D)

@@ -619,3 +619,17 @@ def test_the_widest_windows_and_tokens_before_the_first_position(fmt, q_lens, kv
             o, lse = KV.attention(q, b.cache, *b.args(), causal=causal, window=window, return_lse=True)
             R.check_attention(b, q, o, lse, causal=causal, window=window, label=f"{window} {causal}")
     assert b.cache.get_status() == S.OK
+
+
+def test_more_rows_than_an_int_counts_are_refused():
+    # broadcast rows, so that no memory is behind them
+    b = R.Batch("bf16", 2, 64, 16, [3], [3], fill=False)
+    one = torch.zeros((1, 2, 64), dtype=torch.bfloat16, device="cuda")
+    for n in (2 ** 31, 2 ** 32 + 3):
+        many = one.expand(n, 2, 64)
+        for call in (lambda: KV.append(b.cache, many, many, *b.args()), lambda: KV.attention(many, b.cache, *b.args())):
+            with pytest.raises(S.SageFp4Error) as e:
+                call()
+            assert e.value.code == S.EINVAL
+    torch.cuda.synchronize()
+    assert torch.isnan(b.cache.k_codes).all() and b.cache.get_status() == S.OK
