@@ -52,13 +52,18 @@ inline bool take_strides(const sage_fp4_strides& in, int64_t B, int64_t H, int64
   return true;
 }
 
-// Read and reset a status word after the stream's work.
+// Read and reset a status word after the stream's work, on that stream alone:
+// the default stream may be busy with something else, and a reset there could
+// come after a later call's error.
 inline int read_status(int32_t* status, void* stream) {
   if (!is_aligned(status, 4)) return SAGE_FP4_EINVAL;
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return SAGE_FP4_ECUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
   int32_t h = 0;
-  if (cudaMemcpy(&h, status, sizeof(h), cudaMemcpyDeviceToHost) != cudaSuccess) return SAGE_FP4_ECUDA;
-  if (h != 0 && cudaMemset(status, 0, sizeof(h)) != cudaSuccess) return SAGE_FP4_ECUDA;
+  if (cudaMemcpyAsync(&h, status, sizeof(h), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
+    return SAGE_FP4_ECUDA;
+  if (h != 0 && (cudaMemsetAsync(status, 0, sizeof(h), st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess))
+    return SAGE_FP4_ECUDA;
   return h;
 }
 

@@ -633,3 +633,14 @@ def test_more_rows_than_an_int_counts_are_refused():
             assert e.value.code == S.EINVAL
     torch.cuda.synchronize()
     assert torch.isnan(b.cache.k_codes).all() and b.cache.get_status() == S.OK
+
+
+def test_a_status_is_read_on_its_own_stream():
+    # while the default stream is busy with something else
+    b = R.Batch("bf16", 2, 64, 16, [3], [3])
+    side = torch.cuda.Stream()
+    b.cache.status[0] = S.EINDEX
+    torch.cuda.synchronize()
+    torch.cuda._sleep(500_000_000)
+    assert b.cache.get_status(side) == S.EINDEX and b.cache.get_status(side) == S.OK
+    assert not torch.cuda.current_stream().query()

@@ -384,3 +384,15 @@ def test_forward_mode_is_refused():
                 Q.norm_rope(x[0], x[1], p, table, x[2], x[3])
     with pytest.raises(RuntimeError):
         torch.func.jvp(lambda x: Q.norm_rope(x, k, p, table, *w)[0], (q.contiguous(),), (torch.ones_like(q),))
+
+
+def test_a_status_is_read_on_its_own_stream():
+    # while the default stream is busy with something else
+    table = Q.rope_table(8, 64)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    table.status[0] = S.EINDEX
+    torch.cuda.synchronize()
+    torch.cuda._sleep(500_000_000)
+    assert table.get_status(side) == S.EINDEX and table.get_status(side) == S.OK
+    assert not torch.cuda.current_stream().query()
