@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/sage_fp4.h"
 #include "kernels.h"
 
@@ -15,24 +17,25 @@ inline bool is_aligned(const void* p, uintptr_t a) { return p && (reinterpret_ca
 // The current device is an sm_103 one (the kernels are compiled for sm_103a
 // only); its number of SMs in *sms.
 inline int check_device_103(int* sms) {
-  struct Seen {
-    int state, sms;  // state: 0 unknown, 1 supported, 2 not
-  };
-  static Seen cache[64];  // racing threads write the same values
+  // 0 unknown, -1 not supported, else the number of SMs: one word, so that a
+  // thread sees all of what another found out, or nothing
+  static std::atomic<int> cache[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return SAGE_FP4_ECUDA;
   if (dev < 0 || dev >= 64) return SAGE_FP4_EUNSUPPORTED;
-  if (!cache[dev].state) {
-    int major = 0, minor = 0, n = 0;
+  int n = cache[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
+    int major = 0, minor = 0;
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return SAGE_FP4_ECUDA;
-    cache[dev].sms = n;
-    cache[dev].state = (major == 10 && minor == 3) ? 1 : 2;
+    if (major != 10 || minor != 3) n = -1;
+    cache[dev].store(n, std::memory_order_relaxed);
   }
-  *sms = cache[dev].sms;
-  return cache[dev].state == 1 ? SAGE_FP4_OK : SAGE_FP4_EUNSUPPORTED;
+  if (n < 0) return SAGE_FP4_EUNSUPPORTED;
+  *sms = n;
+  return SAGE_FP4_OK;
 }
 
 // A stride triple for the kernels: >= 0, multiples of 8 elements (16-byte

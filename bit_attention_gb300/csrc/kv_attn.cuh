@@ -186,12 +186,12 @@ cudaError_t launch_after(void (*kernel)(A...), dim3 grid, int threads, int share
 // Allow a kernel its dynamic shared memory, once for each device.
 template <auto kKernel>
 cudaError_t set_shared_once(int bytes) {
-  static bool done[64];  // racing threads set the same attribute
+  static std::atomic<bool> done[64];  // racing threads set the same attribute
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || (dev >= 0 && dev < 64 && done[dev])) return e;
+  if (e != cudaSuccess || (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire))) return e;
   e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev].store(true, std::memory_order_release);
   return e;
 }
 

@@ -644,3 +644,39 @@ def test_a_status_is_read_on_its_own_stream():
     torch.cuda._sleep(500_000_000)
     assert b.cache.get_status(side) == S.EINDEX and b.cache.get_status(side) == S.OK
     assert not torch.cuda.current_stream().query()
+
+
+def test_first_calls_from_many_threads():
+    # of a process: what the library notes of a device is noted by one of them
+    import subprocess
+    import sys
+    code = """
+import sys, threading
+sys.path[:0] = ["tests", "."]
+import kv_reference as R, torch
+from bit_attention_gb300 import kv_cache as KV, sage_fp4 as S
+shapes = [([1, 1], [70, 300]), ([150, 3], [150, 40])]
+n = 16
+outs = [None] * n
+S.load()
+torch.zeros(1, device="cuda")
+start, bad = threading.Barrier(n), []
+def work(i):
+    try:
+        start.wait()
+        b = R.Batch("e4m3", 2, 64, 16, *shapes[i % 2], seed=i % 2)
+        q = torch.ones((b.T, 8, 64), dtype=torch.bfloat16, device="cuda")
+        outs[i] = KV.attention(q, b.cache, *b.args())
+        assert b.cache.get_status() == S.OK
+    except BaseException as e:
+        bad.append(e)
+threads = [threading.Thread(target=work, args=(i,)) for i in range(n)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+torch.cuda.synchronize()
+assert not bad, bad
+assert all(torch.equal(outs[i], outs[i % 2]) for i in range(n))
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=__file__.rsplit("/tests/", 1)[0])
+    assert r.returncode == 0, r.stderr[-2000:]
