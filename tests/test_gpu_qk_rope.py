@@ -396,3 +396,20 @@ def test_a_status_is_read_on_its_own_stream():
     torch.cuda._sleep(500_000_000)
     assert table.get_status(side) == S.EINDEX and table.get_status(side) == S.OK
     assert not torch.cuda.current_stream().query()
+
+
+def test_gradients_through_sagebwd_are_those_of_the_calls_by_hand():
+    # autograd through norm_rope and the 8-bit attention against both backward calls
+    from bit_attention_gb300 import sagebwd as SB
+    rng, q, k, w = case(17, 1, 256, 2, 2, 64)
+    v = bf16(rng.standard_normal((1, 2, 256, 64))).requires_grad_()
+    leaves = [x.detach().clone().requires_grad_() for x in (q, k, *w)]
+    table = Q.rope_table(256, 64)
+    p = torch.arange(256, dtype=torch.int32, device="cuda")
+    o = SB.attention(*Q.norm_rope(leaves[0], leaves[1], p, table, leaves[2], leaves[3], out_layout="HND"), v, causal=True)
+    do = torch.randn_like(o)
+    o.backward(do)
+    y = [x.detach().requires_grad_() for x in Q.forward(q, k, p, table, *w, out_layout="HND")]
+    SB.attention(*y, v.detach(), causal=True).backward(do)
+    by_hand = Q.backward(y[0].grad, y[1].grad, q, k, p, table, *w, grad_layout="HND")
+    assert all(torch.equal(x.grad, g) for x, g in zip(leaves, by_hand))
