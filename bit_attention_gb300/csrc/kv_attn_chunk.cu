@@ -68,8 +68,8 @@ struct Smem {
   static constexpr int kMask = kBar + 32 * 8;         // [8 tiles][4] words: keys that exist
   static constexpr int kScale = kMask + 8 * 16;       // [8 tiles][4] log2 of V's scale of 32 keys (E4M3)
   static constexpr int kKScale = kScale + 8 * 16;     // [8 tiles][4] K's scale of 32 keys (E4M3)
-  static constexpr int kMisc = kKScale + 8 * 16;        // tensor-memory address, abort flag
-  static constexpr int kAlloc = kMisc + 16 + 1024;    // with room to align to 1024
+  static constexpr int kMisc = kKScale + 8 * 16;        // tensor-memory address, abort flag, pieces to redo [8 softmax warps]
+  static constexpr int kAlloc = kMisc + 48 + 1024;    // with room to align to 1024
 };
 static_assert(Smem<128>::kAlloc <= 227 * 1024 && Smem<64>::kAlloc <= 227 * 1024, "shared memory");
 
@@ -233,6 +233,106 @@ __device__ __forceinline__ void copy_rows(uint32_t tile, int base, const uint8_t
   }
 }
 
+// ------------------------------------------------------------------ rows of huge scores
+// The tile loop takes a row's reference from a score times its factor with one
+// rounding, the sum of that and P's raise with another.  Beyond 2^19 (log2
+// units) these no longer leave P's exponents where FP16 and FP32 hold them.  Pieces
+// of a warp's rows in which a reference ends there, or whose sum or O an infinite
+// weight has gone through (every channel of O then), are done again here, a row at a
+// time: every score is rounded first and the largest subtracted before anything
+// else.  So it is for any row of finite scores; how long it takes matters little,
+// while a second path in the tile loop cost 2 to 9% of that.
+constexpr float kHuge = 0x1p19f;
+
+// Of the piece that the walk is at, the warp's rows from `at` of the entry on;
+// results go where the tile loop's went.
+template <int kFmt, int D>
+__device__ __forceinline__ void redo_rows(const KvView& c, const AttnArgs& a, const AttnWork& work, const Walk& walk, int at) {
+  constexpr int kC = D / 8, kG = 32 / kC;
+  const int lane = threadIdx.x & 31, ch = lane % kC, grp = lane / kC;
+  const int slot = walk.first && walk.last ? -1 : 2 * static_cast<int>(blockIdx.x) + (walk.first ? 1 : 0);
+  const PlanEntry en = walk.entry(work);
+  const int b = en.b, h = walk.h;
+  auto each = [](const uint4& u, float (&f)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  };
+  for (int r = 0; r < 32 && at + r < entry_rows(en, a.G); r++) {
+    const int rr = en.row0 + at + r, i = rr / a.G, hq = h * a.G + rr - i * a.G;
+    const long long tok = en.q0 + i;
+    const uint16_t* qr = a.q + tok * a.qr.t + hq * a.qr.h;
+    const int2 see = key_range(a, en.len, en.nq, i);
+    const int first = max(walk.t * kTile, see.x), end = min((walk.t + walk.tiles) * kTile, see.y);
+    float top = -INFINITY, l = 0.0f, o[8] = {};
+    for (int j0 = first; j0 < end; j0 += 32) {
+      // a lane's key, then a lane group's channels of every kG-th key's value
+      const long long row = j0 + lane < end ? row_of(c, b, h, j0 + lane) : -1;
+      float s = row >= 0 ? 0.0f : -INFINITY;
+#pragma unroll 1
+      for (int x = 0; x < kC; x++) {
+        float k[8], f[8];
+        each(*reinterpret_cast<const uint4*>(qr + 8 * x), f);
+        each(row >= 0 ? load_chunk<kFmt, D>(c.kc, c.ks, row, x) : uint4{0, 0, 0, 0}, k);
+#pragma unroll
+        for (int e = 0; e < 8; e++) s = fmaf(f[e], k[e], s);
+      }
+      s = row >= 0 ? __fmul_rn(s, a.scale_log2) : -INFINITY;
+      float to = s;
+#pragma unroll
+      for (int i = 16; i > 0; i >>= 1) to = fmaxf(to, __shfl_xor_sync(kAll, to, i));
+      to = fmaxf(top, to);
+      if (to == -INFINITY) continue;
+      const float alpha = ex2_approx(top - to), p = ex2_approx(s - to);
+      top = to;
+      l = fmaf(l, alpha, p);  // a lane's own keys
+#pragma unroll
+      for (int e = 0; e < 8; e++) o[e] *= alpha;
+#pragma unroll 1
+      for (int i = grp; i < 32; i += kG) {
+        const long long vr = __shfl_sync(kAll, row, i);
+        const float pi = __shfl_sync(kAll, p, i);
+        float v[8];
+        each(vr >= 0 ? load_chunk<kFmt, D>(c.vc, c.vs, vr, ch) : uint4{0, 0, 0, 0}, v);
+#pragma unroll
+        for (int e = 0; e < 8; e++) o[e] = fmaf(pi, v[e], o[e]);
+      }
+    }
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) {
+      l += __shfl_xor_sync(kAll, l, i);
+#pragma unroll
+      for (int e = 0; e < 8; e++) o[e] += i >= kC ? __shfl_xor_sync(kAll, o[e], i) : 0.0f;
+    }
+    if (slot < 0) {
+      const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+      uint16_t* dst = a.o + tok * a.orow.t + hq * a.orow.h + 8 * ch;
+      if (grp == 0)
+        *reinterpret_cast<uint4*>(dst) = uint4{bf2(o[0] * inv, o[1] * inv), bf2(o[2] * inv, o[3] * inv),
+                                               bf2(o[4] * inv, o[5] * inv), bf2(o[6] * inv, o[7] * inv)};
+      if (a.lse && lane == 0) a.lse[tok * a.Hq + hq] = l > 0.0f ? (top + lg2_approx(l)) * kLn2 : -INFINITY;
+    } else {
+      float4* part = reinterpret_cast<float4*>(work.part_o) + static_cast<size_t>(slot) * (D / 4) * kRows + at + r;
+      if (grp == 0) {
+        part[static_cast<size_t>(2 * ch) * kRows] = float4{o[0], o[1], o[2], o[3]};
+        part[static_cast<size_t>(2 * ch + 1) * kRows] = float4{o[4], o[5], o[6], o[7]};
+      }
+      if (lane == 0) work.part_ml[static_cast<size_t>(slot) * kRows + at + r] = float2{top, l};
+    }
+  }
+}
+
+// Of all the CTA's pieces, those whose bit is set (the last bit: of the 32nd and all
+// after it), once the tile loops are through and nobody waits for this warp.
+template <int kFmt, int D>
+__device__ __noinline__ void redo_pieces(const KvView& c, const AttnArgs& a, const AttnWork& work, uint32_t pieces, int at) {
+  Walk walk(work, c.H, blockIdx.x);
+  for (int n = 0; walk.next(work);) {
+    if (walk.tiles == 0 || (at & 128) >= entry_rows(walk.entry(work), a.G)) continue;
+    if ((pieces >> min(n++, 31)) & 1) redo_rows<kFmt, D>(c, a, work, walk, at);
+  }
+}
+
 // ------------------------------------------------------------------ kernel
 template <int kFmt, int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -245,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) { return sbase + L::kBar + 8 * i; };
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+  uint32_t* lost = reinterpret_cast<uint32_t*>(smem + L::kMisc + 16);
   uint32_t* mask = reinterpret_cast<uint32_t*>(smem + L::kMask);
   float* vlog = reinterpret_cast<float*>(smem + L::kScale);
   float* kscale = reinterpret_cast<float*>(smem + L::kKScale);
@@ -269,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(bar(B_DRAIN), 1);
     *abort = 0;
+    for (int i = 0; i < 8; i++) lost[i] = 0;
     mbar_fence_init();
   }
   if (warp == 12) {
@@ -534,13 +636,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (cur.out >= 0) work.part_ml[static_cast<size_t>(cur.slot) * kRows + r] = float2{l > 0.0f ? base : -INFINITY, l};
         }
+        uint32_t o[8];
+        __syncwarp();
+        tmem_ld8(tO, o);
+        tmem_wait_ld();
         pieces++;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_OFREE + m));
+        const bool gone = fabsf(ref) > kHuge || !(l < INFINITY) || !(fabsf(__uint_as_float(o[0])) < INFINITY);
+        if (__any_sync(kAll, cur.out >= 0 && ref != -INFINITY && gone) && lane == 0) lost[warp] |= 1u << min(pieces - 1, 31);
       }
       cur = next;
     }
+    __syncwarp();
+    if (ok && lost[warp]) redo_pieces<kFmt, D>(c, a, work, lost[warp], 128 * m + 32 * (warp & 3));
     tc_fence_before();
   } else if (wg == 2) {
     // ---- gather: warp w of four takes keys 32 w .. of every tile

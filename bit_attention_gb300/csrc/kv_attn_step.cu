@@ -3,7 +3,8 @@
 // once for all query heads of its group.
 //
 // The unit of work is a warp, which walks its own share of the KV tiles and
-// shares nothing with other warps: no shared memory, no waits.  It takes up to
+// shares nothing with other warps: its buffers in shared memory are its own, and
+// it waits for its own copies alone.  It takes up to
 // 8 * kNt query rows (new tokens x heads of the group) against kKeys keys a
 // step, with warp-level MMAs in the transposed form that wastes nothing on
 // eight rows: S^T = K Q^T (M = keys, N = rows), O^T += V^T P^T (M = channels,
@@ -436,7 +437,10 @@ __global__ void __launch_bounds__(kThreads, kNt == 1 ? 3 : 2)
       for (int n = 0; n < kNt; n++)
 #pragma unroll
         for (int x = 0; x < 4; x++) o[t][n][x] = 0.0f;
-    // what the row sum is relative to, this lane's part of it, what P is relative to (log2)
+    // The largest score so far (log2 units), which weights are relative to, and this
+    // lane's part of their sum; E4M3: the largest of score - m + log2 of V's scale,
+    // which P is relative to besides.  A score of any size is subtracted first:
+    // what remains is small, and nothing is lost by adding to that.
     float m[kNt][2], l[kNt][2], mw[kNt][2];
 #pragma unroll
     for (int n = 0; n < kNt; n++)
@@ -509,25 +513,29 @@ __global__ void __launch_bounds__(kThreads, kNt == 1 ? 3 : 2)
       // outgrown its own by kGrow: FP16's range has room for that, and most
       // steps then need one vote instead of reductions over the lanes.
       uint32_t p[kG][kNt][2];
-      float top[kNt][2], topw[kNt][2];
+      auto or_zero = [](float x) { return x == -INFINITY ? 0.0f : x; };
+      // the largest s - sub + log2 of V's scale of a row among this lane's keys
+      auto with_scale = [&](int n, int y, float sub) {
+        float t = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kG; i++)
+          t = max3f(t, (s[i][n][y] - sub) + vx[kVScale ? i : 0][0], (s[i][n][2 + y] - sub) + vx[kVScale ? i : 0][1]);
+        return t;
+      };
+      float top[kNt][2];
       bool grown = false;
 #pragma unroll
       for (int n = 0; n < kNt; n++)
 #pragma unroll
         for (int y = 0; y < 2; y++) {
-          float t = -INFINITY, tw = -INFINITY;
+          float t = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < kG; i++) {
-            t = max3f(t, s[i][n][y], s[i][n][2 + y]);
-            if constexpr (kVScale) tw = max3f(tw, s[i][n][y] + vx[i][0], s[i][n][2 + y] + vx[i][1]);
-          }
+          for (int i = 0; i < kG; i++) t = max3f(t, s[i][n][y], s[i][n][2 + y]);
           top[n][y] = t;
-          if constexpr (kVScale) {
-            topw[n][y] = tw;
-            grown |= tw > mw[n][y] + kGrow || t > m[n][y] + 64.0f;
-          } else {
+          if constexpr (kVScale)
+            grown |= with_scale(n, y, or_zero(m[n][y])) > mw[n][y] + kGrow || t > m[n][y] + 16.0f;
+          else
             grown |= t > m[n][y] + kGrow;
-          }
         }
       if (__any_sync(kAll, grown)) {
 #pragma unroll
@@ -535,13 +543,15 @@ __global__ void __launch_bounds__(kThreads, kNt == 1 ? 3 : 2)
 #pragma unroll
           for (int y = 0; y < 2; y++) {
             const float t = fmaxf(m[n][y], over_keys_max(top[n][y]));
-            const float al = t == -INFINITY ? 1.0f : ex2_approx(m[n][y] - t);  // 0 on the row's first keys
+            const float d = t == -INFINITY ? 0.0f : m[n][y] - t, al = ex2_approx(d);  // 0 on the row's first keys
             m[n][y] = t;
             l[n][y] *= al;
             float aw = al;
             if constexpr (kVScale) {
-              const float tw = fmaxf(mw[n][y], over_keys_max(topw[n][y]));
-              aw = tw == -INFINITY ? 1.0f : ex2_approx(mw[n][y] - tw);
+              // O's reference, relative to the new maximum, before and after
+              const float old = mw[n][y] == -INFINITY ? -INFINITY : mw[n][y] + d;
+              const float tw = fmaxf(old, over_keys_max(with_scale(n, y, or_zero(t))));
+              aw = tw == -INFINITY ? 1.0f : ex2_approx(old - tw);
               mw[n][y] = tw;
             }
 #pragma unroll
@@ -552,15 +562,17 @@ __global__ void __launch_bounds__(kThreads, kNt == 1 ? 3 : 2)
       for (int n = 0; n < kNt; n++)
 #pragma unroll
         for (int y = 0; y < 2; y++) {
-          const float sub = (m[n][y] == -INFINITY ? 0.0f : m[n][y]) - (kVScale ? 0.0f : kRaise);
-          const float subw = kVScale ? (mw[n][y] == -INFINITY ? 0.0f : mw[n][y]) - kRaise : 0.0f;
+          const float sub = or_zero(m[n][y]);
+          const float subw = kVScale ? or_zero(mw[n][y]) - kRaise : 0.0f;
 #pragma unroll
           for (int i = 0; i < kG; i++) {
-            const float p0 = ex2_approx(s[i][n][y] - sub), p1 = ex2_approx(s[i][n][2 + y] - sub);
+            float d0 = s[i][n][y] - sub, d1 = s[i][n][2 + y] - sub;
+            if constexpr (!kVScale && kRaise != 0.0f) d0 += kRaise, d1 += kRaise;
+            const float p0 = ex2_approx(d0), p1 = ex2_approx(d1);
             l[n][y] += p0 + p1;
             if constexpr (kVScale) {
-              s[i][n][y] = ex2_approx(s[i][n][y] + (vx[i][0] - subw));
-              s[i][n][2 + y] = ex2_approx(s[i][n][2 + y] + (vx[i][1] - subw));
+              s[i][n][y] = ex2_approx(d0 + (vx[i][0] - subw));
+              s[i][n][2 + y] = ex2_approx(d1 + (vx[i][1] - subw));
             } else {
               s[i][n][y] = p0, s[i][n][2 + y] = p1;
             }
@@ -616,14 +628,14 @@ __global__ void __launch_bounds__(kThreads, kNt == 1 ? 3 : 2)
     for (int n = 0; n < kNt; n++)
 #pragma unroll
       for (int y = 0; y < 2; y++) {
-        const float sum = over_keys_sum(l[n][y]);
+        // the sum and o relative to the row's maximum (the first raised, but for E4M3)
+        const float up = kVScale ? 1.0f : __uint_as_float((127u - static_cast<uint32_t>(kRaise)) << 23);
+        const float sum = over_keys_sum(l[n][y]) * up;
         const int r = 8 * n + 2 * q + y;
         if (r >= rows) continue;
-        // o relative to the row maximum that l is relative to
-        const float top = kVScale ? m[n][y] : m[n][y] - kRaise;
-        float f = sum > 0.0f ? 1.0f : 0.0f;
+        float f = sum > 0.0f ? up : 0.0f;
         if constexpr (kVScale)
-          if (sum > 0.0f) f = ex2_approx(mw[n][y] - kRaise - m[n][y]);
+          if (sum > 0.0f) f = ex2_approx(mw[n][y] - kRaise);
         if (whole) {
           if (sum > 0.0f) f *= 1.0f / sum;
           const int rr = e.row0 + r, i = rr / a.G, gq = rr - i * a.G;
@@ -635,14 +647,14 @@ __global__ void __launch_bounds__(kThreads, kNt == 1 ? 3 : 2)
             *reinterpret_cast<uint4*>(dst + channel(t)) =
                 uint4{bf2(o[t][n][y] * f, o[t][n][2 + y] * f), bf2(o[t + 1][n][y] * f, o[t + 1][n][2 + y] * f),
                       bf2(o[t + 2][n][y] * f, o[t + 2][n][2 + y] * f), bf2(o[t + 3][n][y] * f, o[t + 3][n][2 + y] * f)};
-          if (a.lse && g == 0) a.lse[tok * a.Hq + hq] = sum > 0.0f ? (top + lg2_approx(sum)) * kLn2 : -INFINITY;
+          if (a.lse && g == 0) a.lse[tok * a.Hq + hq] = sum > 0.0f ? (m[n][y] + lg2_approx(sum)) * kLn2 : -INFINITY;
         } else {
           float* dst = work.part_o + (slot * kRows + r) * D;
 #pragma unroll
           for (int t = 0; t < kTiles; t += 2)
             *reinterpret_cast<float4*>(dst + channel(t)) =
                 float4{o[t][n][y] * f, o[t][n][2 + y] * f, o[t + 1][n][y] * f, o[t + 1][n][2 + y] * f};
-          if (g == 0) work.part_ml[slot * kRows + r] = float2{sum > 0.0f ? top : -INFINITY, sum};
+          if (g == 0) work.part_ml[slot * kRows + r] = float2{m[n][y], sum};
         }
       }
   }

@@ -111,7 +111,8 @@ size_t sage_kv_attn_workspace_bytes(const sage_kv_cache *cache, int B, int T, in
  * causal = 1: a query at position p sees the tokens j <= p; 0: all kv_len.
  * window > 0: only j > p - window; 0: no window.  A row that sees nothing gets
  * o = 0 and lse = -inf.  scale: positive, at most 1e30.  Sums and softmax
- * statistics are FP32.  workspace: 256-byte aligned, no initialisation; calls
+ * statistics are FP32; a score may be of any size that FP32 holds (rows beyond
+ * 2^18 are far slower where a call has many rows).  workspace: 256-byte aligned, no initialisation; calls
  * sharing one must be ordered. */
 int sage_kv_attn(const sage_kv_cache *cache, const sage_kv_batch *batch, const void *q, sage_kv_rows q_rows, void *o,
                  sage_kv_rows o_rows, float *lse, int T, int Hq, int causal, int window, float scale, void *workspace,

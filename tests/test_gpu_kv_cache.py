@@ -680,3 +680,69 @@ assert all(torch.equal(outs[i], outs[i % 2]) for i in range(n))
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
                        cwd=__file__.rsplit("/tests/", 1)[0])
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_lens,kv_lens", [([2, 1], [300, 90]), ([140, 20], [300, 90]), ([2, 70], [9000, 70])])
+def test_scores_of_any_size(fmt, D, q_lens, kv_lens):
+    # one-hot keys of several sizes and queries that hit one channel: scores from
+    # 2^8 to 2^100 and below 0, where FP32 has no digits left for what is added to
+    # one.  A score is one product, rounded three times in FP32: within 2^-22 of
+    # itself.  Keys that lie nearer than that to the row's largest (and 100 for
+    # what underflows) may share its weight in any way.
+    n, H, G = sum(kv_lens), 1, 8
+    b = R.Batch(fmt, H, D, 64, q_lens, kv_lens, seed=30, fill=False)
+    k = np.zeros((n, H, D))
+    k[np.arange(n), 0, np.arange(n) % D] = np.array([4.0, 6.0, 8.0, 7.0, 12.0])[np.arange(n) // D % 5]
+    cu = torch.from_numpy(np.concatenate([[0], np.cumsum(kv_lens)]).astype(np.int32)).cuda()
+    KV.append(b.cache, bf16(k), bf16(b.rng.standard_normal((n, H, D))), cu, b.kv_len, b.block_table)
+    t, h = np.indices((b.T, G))
+    alone = 0
+    for size in (2.0 ** 8, 2.0 ** 17, 2.0 ** 20, 2.0 ** 24, 2.0 ** 31, 2.0 ** 60, 2.0 ** 100):
+        q = np.zeros((b.T, G, D))
+        q[t, h, b.rng.integers(0, D, t.shape)] = size * b.rng.choice([-1.0, 1.0], t.shape) * b.rng.uniform(0.5, 1.0, t.shape)
+        q = bf16(q)
+        o, lse = (R.f64(x) for x in KV.attention(q, b.cache, *b.args(), return_lse=True))
+        q = R.f64(q)
+        for s, (nq, m) in enumerate(zip(q_lens, kv_lens)):
+            kd, vd = b.dense("k", s)[0], b.dense("v", s)[0]
+            for i in range(nq):
+                seen = m - nq + i + 1
+                x = q[b.cu[s] + i] @ kd[:seen].T * D ** -0.5
+                top = x.max(-1)
+                for g in range(G):
+                    near = x[g] >= top[g] - 100 - 2.0 ** -20 * abs(top[g])
+                    v, got = vd[:seen][near], o[b.cu[s] + i, g]
+                    edge = 2.0 ** -6 * np.abs(v).max(0)  # a weight's rounding, a result's
+                    alone += near.sum() == 1
+                    assert (got >= v.min(0) - edge).all() and (got <= v.max(0) + edge).all(), (size, s, i, g)
+                    assert abs(lse[b.cu[s] + i, g] - top[g]) <= 2.0 ** -20 * abs(top[g]) + np.log(near.sum()) + 1e-5, (size, s, i, g)
+    assert alone > 0 and b.cache.get_status() == S.OK
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("q_lens,kv_lens", [([2, 1], [700, 300]), ([150, 90], [700, 300]), ([1, 40], [5000, 300])])
+def test_scores_that_change_from_huge_to_small_and_back(fmt, q_lens, kv_lens):
+    # stretches of 150 keys whose scores are all -A, 0, A or 2A for every query of a
+    # head: the last kind that a row sees takes it all, equally
+    D, H, G, n = 64, 1, 8, sum(kv_lens)
+    b = R.Batch(fmt, H, D, 16, q_lens, kv_lens, seed=31, fill=False)
+    k = np.zeros((n, H, D))
+    order = np.concatenate([np.arange(m) // 150 % 4 for m in kv_lens])
+    k[:, 0, 0] = np.array([-4.0, 0.0, 4.0, 8.0])[order]
+    cu = torch.from_numpy(np.concatenate([[0], np.cumsum(kv_lens)]).astype(np.int32)).cuda()
+    KV.append(b.cache, bf16(k), bf16(b.rng.standard_normal((n, H, D))), cu, b.kv_len, b.block_table)
+    q = np.zeros((b.T, G, D))
+    q[:, :, 0] = 2.0 ** np.array([10, 20, 22, 26, 30, 40, 70, 100])
+    for sign in (1.0, -1.0):
+        o = R.f64(KV.attention(bf16(sign * q), b.cache, *b.args()))
+        for s, (nq, m) in enumerate(zip(q_lens, kv_lens)):
+            kd, vd = b.dense("k", s)[0], b.dense("v", s)[0]
+            for i in range(nq):
+                x = sign * kd[:m - nq + i + 1, 0]
+                v = vd[:m - nq + i + 1][x == x.max()]
+                # weights alike but for a rounding each (2^-8), and the result's; FP32 sums of up to 2^12 terms
+                tol = (2.0 ** -8 * 1.01 + 2.0 ** -12) * (np.abs(v).mean(0) + np.abs(v.mean(0)))
+                assert (np.abs(o[b.cu[s] + i] - v.mean(0)) <= tol).all(), (sign, s, i)
+    assert b.cache.get_status() == S.OK
