@@ -28,8 +28,8 @@
 // pair instead of six (measured on 128 keys of E4M3: 840 cycles a tile instead
 // of 2050): E2M1 codes times E4M3 scales are exact there, and E4M3 codes are
 // multiplied by their scale relative to the largest scale of 32 keys (a warp's
-// share of a tile; exact down to 2^-15 of it, 2^-25 of it below), whose exponent
-// enters the scores (K) or P's exponent (V).  Q's rows are scaled by the power
+// share of a tile), whose exponent enters the scores (K) or P's exponent (V); Scales
+// below says where that is exact and what else is done.  Q's rows are scaled by the power
 // of two that brings their largest magnitude to 2^14 .. 2^15: bf16's eight bits
 // fit while a channel is above 2^-28 of it.  P is rounded to bf16 (2^-8
 // relative) or FP16 (weights of 2^7 at the reference: 2^-12 relative down to
@@ -67,8 +67,11 @@ struct Smem {
   static constexpr int kBar = kStage + 8 * 4096;
   static constexpr int kMask = kBar + 32 * 8;         // [8 tiles][4] words: keys that exist
   static constexpr int kScale = kMask + 8 * 16;       // [8 tiles][4] log2 of V's scale of 32 keys (E4M3)
-  static constexpr int kKScale = kScale + 8 * 16;     // [8 tiles][4] K's scale of 32 keys (E4M3)
-  static constexpr int kMisc = kKScale + 8 * 16;        // tensor-memory address, abort flag, pieces to redo [8 softmax warps]
+  static constexpr int kKScale = kScale + 8 * 16;     // [8 tiles][4] K's scale of 32 keys (E4M3), 0: wide
+  static constexpr int kBytes = kKScale + 8 * 16;     // [kInfo tiles][2][128] scale bytes of K and V (E4M3, wide rows)
+  static constexpr int kInfo = D == 64 ? 8 : 4;       // (a tile's are read before the one three tiles on is written)
+  static constexpr int kMisc = kBytes + kInfo * 256;        // tensor-memory address, abort flag, spread of
+                                                           // V's scales [2], pieces to redo [8 softmax warps]
   static constexpr int kAlloc = kMisc + 48 + 1024;    // with room to align to 1024
 };
 static_assert(Smem<128>::kAlloc <= 227 * 1024 && Smem<64>::kAlloc <= 227 * 1024, "shared memory");
@@ -143,11 +146,14 @@ struct Gather {
   uint32_t code[kSteps][kWords];
   uint32_t scale[kFmt == kNvfp4 ? kSteps : 1];  // E4M3: of the lane's own row; NVFP4: of its pieces
 
+  // E4M3: the scale of the lane's own row, -1: none (asked for before the codes, which
+  // are wanted later)
+  __device__ __forceinline__ void load_scale(const uint8_t* scales, long long row) { scale[0] = row >= 0 ? scales[row] : 0u; }
+
   // row: this lane's row of the cache (key 32 * warp + lane of the tile), or -1;
   // here: the lanes that have one, of each 16 the first ones
   __device__ __forceinline__ void load(const uint8_t* codes, const uint8_t* scales, long long row, uint32_t here) {
     const int lane = threadIdx.x & 31, q = lane / kLanes, c = lane % kLanes;
-    if constexpr (kFmt == kE4m3) scale[0] = row >= 0 ? scales[row] : 0u;
     const uint8_t *from[2], *sc[2];
 #pragma unroll
     for (int g = 0; g < 2; g++) {
@@ -176,30 +182,16 @@ struct Gather {
     }
   }
 
-  // E4M3: the largest scale byte of the warp's 32 rows, at least 2^-80's: the
-  // row sum, relative to weights that count V's scale, stays within FP32, and
-  // only rows whose largest magnitude is below 2^-95 lose bits by it.
-  __device__ __forceinline__ uint32_t top_scale() const {
-    uint32_t r;
-    asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(r) : "r"(scale[0] < 47u ? 47u : scale[0]));
-    return r;
-  }
-
-  // The rows as FP16 (E4M3: relative to the scale byte `top`) to the tile's rows
-  // from base (a multiple of 32) on.  Chunk ch (8 channels) of row r stands at
+  // The rows as FP16 (E4M3: times `mine`, an FP16 pair, of the lane's own row) to the
+  // tile's rows from base (a multiple of 32) on.  Chunk ch (8 channels) of row r stands at
   // chunk ch ^ (r & 7) of the row's 128 bytes.  For D = 128, where a row's second
   // four lanes write the other half of the tile, those take their pieces' second
   // chunks first, so that eight lanes' 16 bytes fall into eight bank groups.
-  __device__ __forceinline__ void store(uint32_t tile, int base, uint32_t top) const {
+  __device__ __forceinline__ void store(uint32_t tile, int base, uint32_t mine) const {
     const int lane = threadIdx.x & 31, q = lane / kLanes, c = lane % kLanes;
     const bool x = c >= 4;
     const uint32_t rows = tile + (c >> 2) * (128 * 128) + (base + q) * 128;
     const int ch = 2 * (c & 3) + x;
-    uint32_t mine = 0;  // the factor of the lane's own row, an FP16 pair of 2^-d (a missing row's codes are zeros)
-    if constexpr (kFmt == kE4m3) {
-      const int d = static_cast<int>(top - scale[0]);
-      mine = (d < 15 ? (15u - d) << 10 : d < 25 ? 1u << (24 - d) : 0u) * 0x10001u;
-    }
 #pragma unroll
     for (int i = 0; i < kSteps; i++) {
       const uint32_t f = kFmt == kE4m3 ? __shfl_sync(kAll, mine, i * kStep + q) : e4m3_to_h2(scale[kFmt == kNvfp4 ? i : 0]);
@@ -218,6 +210,51 @@ struct Gather {
   }
 };
 
+// E4M3: the scales of a warp's 32 rows of a tile.  Codes are multiplied by 2^7 (so
+// that they use FP16's range) and by their scale relative to the largest of the 32,
+// which enters the scores (K) or P's exponents (V), as long as little is lost by it:
+// K scales within 2^21 (exact in FP16: 18 + 21 bits from 2^15.8 down), V scales within
+// 2^8 or of rows of zeros.  (V's values are exact then; P is relative to the largest
+// weight times that scale and its smallest step 2^-32 of it, so that among 32 values of
+// like sizes a weight is off by 2^-32 of the largest, and by 2^-24 at the limit.)  The
+// others are `wide`: codes are taken without their scales, which the softmax then
+// applies to each key; a tile of these takes six times as long.
+// A scale byte of 17 (a row of zeros, or below 2^-101 in magnitude) is taken for zeros;
+// V's scales count as 2^-80 at least, so that the row sum, relative to weights that
+// count V's scale, stays within FP32, and lower rows lose bits (half a step 2^-112).
+struct Scales {
+  static constexpr uint32_t kZero = 17, kLeastV = 47, kSpreadK = 21, kSpreadV = 8;
+  // a share whose V scales are further apart may leave weights of the least out of
+  // the row sum: its rows are done again
+  static constexpr int kMostV = 92;
+  static constexpr int kBias = 127 + 7;
+  uint32_t top_k, top_v, mine_k, mine_v;  // largest; this lane's factors
+  uint32_t low_v;                         // for kMostV
+  bool wide;
+
+  static __device__ __forceinline__ uint32_t largest(uint32_t v) {
+    uint32_t r;
+    asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(r) : "r"(v));
+    return r;
+  }
+  // 2^(7 - d) as an FP16 pair
+  static __device__ __forceinline__ uint32_t factor(uint32_t d) {
+    return (d < 22 ? (22u - d) << 10 : d < 32 ? 1u << (31 - d) : 0u) * 0x10001u;
+  }
+  // k, v: the lane's scale bytes, 0 where it has no row
+  __device__ __forceinline__ Scales(uint32_t k, uint32_t v) {
+    const bool kz = k <= kZero, vz = v <= kZero;
+    const uint32_t least = v < kLeastV ? kLeastV : v;
+    top_k = largest(kz ? kZero + 1 : k);
+    top_v = largest(least);
+    wide = __any_sync(kAll, (!kz && k + kSpreadK < top_k) || (!vz && least + kSpreadV < top_v));
+    mine_k = kz ? 0u : factor(wide ? 0 : top_k - k);
+    mine_v = vz ? 0u : factor(wide ? least - v : top_v - v);
+    // (a wide share's weights are summed by themselves: only the sum's own range counts)
+    low_v = wide ? 255u - largest(v ? 255u - least : 0u) + 126 - kMostV : top_v;
+  }
+};
+
 // 32 bf16 rows to an operand tile by asynchronous 16-byte copies; a missing
 // row (-1) becomes zeros.
 template <int D>
@@ -231,6 +268,86 @@ __device__ __forceinline__ void copy_rows(uint32_t tile, int base, const uint8_t
     cp_async16(tile + (ch >> 3) * (128 * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src + (off >= 0 ? off : 0) + 16 * ch,
                off >= 0);
   }
+}
+
+// ------------------------------------------------------------------ softmax
+template <int D>
+__device__ __forceinline__ void rescale_o(uint32_t tO, float alpha) {
+#pragma unroll 1
+  for (int j = 0; j < D; j += 8) {
+    uint32_t o[8];
+    tmem_ld8(tO + j, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 8; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+    tmem_st8(tO + j, o);
+  }
+  tmem_wait_st();
+}
+
+struct Row {
+  float ref, l;  // what a thread's row is relative to, its sum
+};
+
+// A tile with wide rows (E4M3), each score by itself: a call that reads them from
+// tensor memory twice, eight at a time, so that the fast path keeps its registers.
+template <int D>
+__device__ __noinline__ Row wide_tile(uint32_t tS, uint32_t tO, uint32_t bar_p, uint32_t info, uint32_t bytes, int see0, int see1, float factor, Row x) {
+  constexpr float kRaise = 7.0f;
+  using L = Smem<D>;
+  const uint32_t mask = info + L::kMask, kscale = info + L::kKScale, vlog = info + L::kScale;
+  // keys c .. c + 7: log2 scores (-inf: not seen), and the exponents of V's scales
+  auto look = [&](int c, float (&u)[8], float (&v)[8]) {
+    uint32_t r[8];
+    tmem_ld8(tS + c, r);
+    const int g = c >> 5;
+    const uint32_t on = (ld_shared4(mask + 4 * g) & bits_below(see1 - 32 * g) & ~bits_below(see0 - 32 * g)) >> (c & 31);
+    const float kf = __uint_as_float(ld_shared4(kscale + 4 * g)), vx = __uint_as_float(ld_shared4(vlog + 4 * g));
+    const uint32_t kb[2] = {ld_shared4(bytes + c), ld_shared4(bytes + c + 4)};
+    const uint32_t vb[2] = {ld_shared4(bytes + 128 + c), ld_shared4(bytes + 128 + c + 4)};
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+      const uint32_t k = (kb[e / 4] >> (8 * (e % 4))) & 255u, w = (vb[e / 4] >> (8 * (e % 4))) & 255u;
+      const float f = kf > 0.0f ? kf : k > Scales::kZero ? __uint_as_float((k + 127 - Scales::kBias) << 23) : 0.0f;
+      v[e] = kf > 0.0f ? vx : static_cast<float>(static_cast<int>(max(w, Scales::kLeastV)) - Scales::kBias);
+      u[e] = (on >> e) & 1 ? __uint_as_float(r[e]) * (factor * f) : -INFINITY;
+    }
+  };
+  float u[8], v[8], top = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < kTile; c += 8) {
+    look(c, u, v);
+#pragma unroll
+    for (int e = 0; e < 8; e++) top = fmaxf(top, u[e] + v[e]);
+  }
+  if (__any_sync(kAll, top > x.ref + kGrow)) {
+    const float to = fmaxf(x.ref, top), alpha = to == -INFINITY ? 1.0f : ex2_approx(x.ref - to);
+    x.ref = to;
+    const bool some = __any_sync(kAll, x.l > 0.0f);
+    x.l *= alpha;
+    if (some) rescale_o<D>(tO, alpha);
+  }
+  const float sub = (x.ref == -INFINITY ? 0.0f : x.ref) - kRaise;
+#pragma unroll 1
+  for (int c = 0; c < kTile; c += 8) {
+    look(c, u, v);
+    uint32_t p[4];
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      const float d0 = u[2 * e] - sub, d1 = u[2 * e + 1] - sub;
+      x.l += ex2_approx(d0) + ex2_approx(d1);
+      p[e] = h2_of(ex2_approx(d0 + v[2 * e]), ex2_approx(d1 + v[2 * e + 1]));
+    }
+    tmem_st4(tS + c / 2, p);  // over scores that have been read
+    if (c % 64 == 56) {
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(bar_p + 8 * (c / 64));
+    }
+  }
+  return x;
 }
 
 // ------------------------------------------------------------------ rows of huge scores
@@ -345,6 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) { return sbase + L::kBar + 8 * i; };
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+  uint32_t* spread = reinterpret_cast<uint32_t*>(smem + L::kMisc + 8);  // V's scales: the largest, 255 less the least
   uint32_t* lost = reinterpret_cast<uint32_t*>(smem + L::kMisc + 16);
   uint32_t* mask = reinterpret_cast<uint32_t*>(smem + L::kMask);
   float* vlog = reinterpret_cast<float*>(smem + L::kScale);
@@ -370,6 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(bar(B_DRAIN), 1);
     *abort = 0;
+    spread[0] = spread[1] = 0;
     for (int i = 0; i < 8; i++) lost[i] = 0;
     mbar_fence_init();
   }
@@ -486,6 +605,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; cur.on && k < cur.tiles; k++, g++) {
         if (!(ok = wait_warp(bar(B_S + m), g & 1, ctl))) break;
         tc_fence_after();
+        if constexpr (kScales) {
+          const float4 f = *reinterpret_cast<const float4*>(kscale + 4 * ((tile0 + k) & 7));
+          if (fminf(fminf(f.x, f.y), fminf(f.z, f.w)) == 0.0f) {
+            const int t = tile0 + k, at = 4 * (t & 7), k0 = (cur.t + k) * kTile;
+            const Row x = wide_tile<D>(tS, tO, bar(B_P + 2 * m), sbase + 4 * at,
+                                       sbase + L::kBytes + 256 * (t % L::kInfo), cur.see.x - k0, cur.see.y - k0, cur.factor,
+                                       Row{ref, l});
+            ref = x.ref, l = x.l;
+            continue;
+          }
+        }
         uint32_t s[4][32];
         float t[4];  // maxima of 32 scores each
 #pragma unroll
@@ -528,19 +658,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float to = fmaxf(ref, top);
           const float alpha = to == -INFINITY ? 1.0f : ex2_approx(ref - to);
           ref = to;
+          const bool some = __any_sync(kAll, l > 0.0f);  // else O holds nothing, or nothing yet
           l *= alpha;
-          if (k > 0) {
-#pragma unroll 1
-            for (int j = 0; j < D; j += 8) {
-              uint32_t o[8];
-              tmem_ld8(tO + j, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 8; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tmem_st8(tO + j, o);
-            }
-            tmem_wait_st();
-          }
+          if (some) rescale_o<D>(tO, alpha);
         }
         const float sub = (ref == -INFINITY ? 0.0f : ref) - kRaise;
 #pragma unroll
@@ -650,7 +770,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       cur = next;
     }
     __syncwarp();
-    if (ok && lost[warp]) redo_pieces<kFmt, D>(c, a, work, lost[warp], 128 * m + 32 * (warp & 3));
+    const bool apart = kScales && static_cast<int>(spread[0] + spread[1]) > 255 + Scales::kMostV;
+    const uint32_t redo = __any_sync(kAll, apart) ? kAll : lost[warp];
+    if (ok && redo) redo_pieces<kFmt, D>(c, a, work, redo, 128 * m + 32 * (warp & 3));
     tc_fence_before();
   } else if (wg == 2) {
     // ---- gather: warp w of four takes keys 32 w .. of every tile
@@ -738,32 +860,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       long long row = row_found();
       uint32_t here = __ballot_sync(kAll, row >= 0);
       if (have) {
+        if constexpr (kScales) gk.load_scale(c.ks, row), gv.load_scale(c.vs, row);
         gk.load(c.kc, c.ks, row, here);
         gv.load(c.vc, c.vs, row, here);
         look_up();
       }
       while (have) {
         if (!(ok = free_slot(n))) break;
-        uint32_t top_k = 0, top_v = 0;
-        if constexpr (kScales) top_k = gk.top_scale(), top_v = gv.top_scale();
-        if (lane == 0) {
-          mask[4 * (tiles & 7) + w] = here;
-          if constexpr (kScales) {
-            kscale[4 * (tiles & 7) + w] = __uint_as_float(top_k << 23);
-            vlog[4 * (tiles & 7) + w] = static_cast<float>(static_cast<int>(top_v) - 127);
+        uint32_t mine_k = 0, mine_v = 0;
+        if constexpr (kScales) {
+          const uint32_t sk = gk.scale[0], sv = gv.scale[0];
+          const Scales x(sk, sv);
+          mine_k = x.mine_k, mine_v = x.mine_v;
+          if (x.wide) {
+            uint8_t* to = smem + L::kBytes + 256 * (tiles % L::kInfo) + 32 * w + lane;
+            to[0] = static_cast<uint8_t>(sk), to[128] = static_cast<uint8_t>(sv);
+          }
+          if (lane == 0) {
+            kscale[4 * (tiles & 7) + w] = x.wide ? 0.0f : __uint_as_float((x.top_k + 127 - Scales::kBias) << 23);
+            vlog[4 * (tiles & 7) + w] = static_cast<float>(static_cast<int>(x.top_v) - Scales::kBias);
+            atomicMax(spread, x.top_v);
+            atomicMax(spread + 1, 255u - x.low_v);
           }
         }
-        gk.store(slot(n), 32 * w, top_k);
+        if (lane == 0) mask[4 * (tiles & 7) + w] = here;
+        gk.store(slot(n), 32 * w, mine_k);
         filled(n++);
         have = more;
         if (have) {
           row = row_found();
           here = __ballot_sync(kAll, row >= 0);
+          if constexpr (kScales) gk.load_scale(c.ks, row), gv.load_scale(c.vs, row);
           gk.load(c.kc, c.ks, row, here);
           look_up();
         }
         if (!(ok = free_slot(n))) break;
-        gv.store(slot(n), 32 * w, top_v);
+        gv.store(slot(n), 32 * w, mine_v);
         filled(n++);
         if (have) gv.load(c.vc, c.vs, row, here);
         tiles++;

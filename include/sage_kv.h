@@ -26,7 +26,10 @@
  *                  nibble, with one E4M3 scale per 16 channels, by the group
  *                  rule of sage_fp4.h (code * scale is a bf16 value).
  * So what a row reads back as is exact in bf16, and attention over a quantized
- * cache is attention over exactly these bf16 values.
+ * cache is attention over exactly these bf16 values, whatever the sizes of the rows
+ * around one and whether they are seen (but E4M3 rows below 2^-101 in magnitude may
+ * count as zeros; where 32 neighbouring values differ by more than 2^8 calls of many
+ * rows take longer).
  *
  * Layout of the buffers (contiguous, 16-byte aligned, k and v alike):
  *   codes  [num_pages][H][page_size][D], [D / 2] bytes for NVFP4;
