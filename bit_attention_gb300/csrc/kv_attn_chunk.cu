@@ -251,7 +251,7 @@ struct Scales {
     mine_k = kz ? 0u : factor(wide ? 0 : top_k - k);
     mine_v = vz ? 0u : factor(wide ? least - v : top_v - v);
     // (a wide share's weights are summed by themselves: only the sum's own range counts)
-    low_v = wide ? 255u - largest(v ? 255u - least : 0u) + 126 - kMostV : top_v;
+    low_v = wide ? min(255u - largest(v ? 255u - least : 0u) + 126u - kMostV, 255u) : top_v;
   }
 };
 

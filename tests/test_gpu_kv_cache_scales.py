@@ -139,6 +139,20 @@ def test_stretches_of_tokens_of_very_different_sizes(D, lens, sizes):
     check(b, bf16(rng.standard_normal((b.T, 4, D))), lens[0][0] > 4)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens", [([2, 1], [3000, 700]), ([130, 70], [3000, 700])])
+@pytest.mark.parametrize("high,low", [(100, -20), (90, -60), (30, -70)])
+def test_stretches_of_mixed_and_of_small_values(D, lens, high, low):
+    # 300 tokens whose values are 2^high and 2^(high - 12) in turn, then 300 of 2^low
+    rng = np.random.default_rng(D + high)
+    n = sum(lens[1])
+    k, v = rng.standard_normal((2, n, 1, D))
+    i = np.arange(n)
+    v *= 2.0 ** np.where(i // 300 % 2 == 0, high - 12.0 * (i % 2), low)[:, None, None]
+    b = filled(k, v, *lens, 1, D, page=32)
+    check(b, bf16(rng.standard_normal((b.T, 4, D))), lens[0][0] > 4)
+
+
 @pytest.mark.parametrize("lens", [FEW, MANY])
 def test_rows_of_zeros_and_next_to_zero(lens):
     # magnitudes down to bf16's smallest, where the scale's byte stops at its least
