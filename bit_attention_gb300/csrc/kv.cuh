@@ -33,11 +33,14 @@ __host__ __device__ constexpr int row_scales(int D) {
 
 __device__ __forceinline__ void flag_index(int32_t* status) { atomicCAS(status, 0, SAGE_FP4_EINDEX); }
 
+// The longest sequence: ends of tiles and of steps past it are ints too.
+constexpr int kMaxLen = INT32_MAX - 4095;
+
 // Tokens of sequence b in the cache, 0 (recorded) for a length that its table
 // cannot hold.
 __device__ __forceinline__ int seq_len(const KvView& c, int b) {
   const int n = c.kv_len[b];
-  if (n >= 0 && n <= (static_cast<long long>(c.max_pages) << c.page_shift)) return n;
+  if (n >= 0 && n <= kMaxLen && n <= (static_cast<long long>(c.max_pages) << c.page_shift)) return n;
   flag_index(c.status);
   return 0;
 }

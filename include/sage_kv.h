@@ -44,7 +44,7 @@
  * Indexes found out of range on the device set *status to SAGE_FP4_EINDEX and
  * are left out: a page outside [0, num_pages) (its tokens are not written, read
  * as zeros, and are not attended to); a kv_len outside [0, max_pages *
- * page_size] (the sequence counts as empty); new tokens outside [0, T] or
+ * page_size] or above 2^31 - 4096 (the sequence counts as empty); new tokens outside [0, T] or
  * fewer than none (the sequence has none).  Where cu_q runs backwards anywhere,
  * any of the batch's new tokens may be left out, and their rows of an output
  * hold anything.

@@ -746,3 +746,23 @@ def test_scores_that_change_from_huge_to_small_and_back(fmt, q_lens, kv_lens):
                 tol = (2.0 ** -8 * 1.01 + 2.0 ** -12) * (np.abs(v).mean(0) + np.abs(v.mean(0)))
                 assert (np.abs(o[b.cu[s] + i] - v.mean(0)) <= tol).all(), (sign, s, i)
     assert b.cache.get_status() == S.OK
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("nq", [1, 100])
+def test_lengths_next_to_the_largest_int_are_recorded_and_left_out(fmt, nq):
+    # a table that repeats a page holds any number of tokens; ends of tiles would not
+    # be ints any more
+    b = R.Batch(fmt, 1, 64, 1024, [nq, nq], [1000, 1000], seed=32)
+    table = b.block_table[:, :1].expand(2, 1 << 21).contiguous()
+    q = bf16(b.rng.standard_normal((b.T, 2, 64)))
+    ref = KV.attention(q, b.cache, b.cu_q, b.kv_len, table)
+    assert b.cache.get_status() == S.OK
+    for n in (2 ** 31 - 1, 2 ** 31 - 100, 2 ** 31 - 4095):
+        lens = b.kv_len.clone()
+        lens[0] = n
+        o, lse = KV.attention(q, b.cache, b.cu_q, lens, table, return_lse=True)
+        assert b.cache.get_status() == S.EINDEX
+        assert (o[:nq] == 0).all() and torch.isneginf(lse[:nq]).all() and torch.equal(o[nq:], ref[nq:])
+        k, v = KV.read(b.cache, lens, table, 64)
+        assert b.cache.get_status() == S.EINDEX and (k[0] == 0).all() and (v[0] == 0).all() and (k[1] != 0).any()
