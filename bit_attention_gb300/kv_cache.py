@@ -229,7 +229,8 @@ def append(cache: PagedCache, k, v, cu_q, kv_len, block_table, stream=None) -> N
 def read(cache: PagedCache, kv_len, block_table, N: int, layout: str = "HND", out=None, stream=None):
     """The first N tokens of every sequence as dense bf16 (k, v) in `layout`
     ("HND" = [B, H, N, D], "NHD" = [B, N, H, D]); tokens past a sequence's
-    length are zeros.  out: (k, v) to write instead of new tensors."""
+    length are zeros.  out: (k, v) to write instead of new tensors, of memory of
+    their own."""
     import torch
     batch = _batch(cache, None, kv_len, block_table)
     if layout not in _fp4.LAYOUTS or not 0 <= N <= INT32_MAX:
@@ -250,6 +251,8 @@ def read(cache: PagedCache, kv_len, block_table, N: int, layout: str = "HND", ou
         _fp4._own_elements(x, nm)
         s = [st if n > 1 else 0 for st, n in zip(x.stride(), shape)]
         strides.append(sage_fp4_strides(s[0], s[1], s[2]) if layout == "HND" else sage_fp4_strides(s[0], s[2], s[1]))
+    if out is not None and k.data_ptr() == v.data_ptr() and k.numel():
+        raise SageFp4Error(EINVAL, "out: k and v share memory")
     _fp4._call(lib().sage_kv_read, "sage_kv_read", cache.index, stream,
                None if stream is None else (k, v, kv_len, block_table, *cache.buffers),
                cache.struct, batch, k.data_ptr(), strides[0], v.data_ptr(), strides[1], N)
@@ -279,7 +282,8 @@ def attention(q, cache: PagedCache, cu_q, kv_len, block_table, causal: bool = Tr
     the last of kv_len[b]); False: all kv_len[b] (cross attention).  window:
     only the last `window` of those.  scale: softmax scale (default
     1/sqrt(D)).  A row that sees nothing is zeros; rows behind cu_q[B] are
-    left as they were.  return_lse: also the natural-log log-sum-exp, float32
+    left as they were.  out: a tensor to write, which shares no memory with q or
+    the cache.  return_lse: also the natural-log log-sum-exp, float32
     [T, Hq] (-inf for a row that sees nothing).  workspace: uint8 tensor of
     attention_workspace_bytes (a temporary one by default); calls sharing one
     must be ordered."""
@@ -298,6 +302,8 @@ def attention(q, cache: PagedCache, cu_q, kv_len, block_table, causal: bool = Tr
         _fp4._own_elements(out, "out")
         if To != T:
             raise SageFp4Error(EINVAL, f"out has {To} rows, q {T}")
+        if T and out.data_ptr() == q.data_ptr():
+            raise SageFp4Error(EINVAL, "out shares memory with q")  # parts of a row are still to be read
     lse = torch.empty((T, Hq), dtype=torch.float32, device=cache.device) if return_lse else None
     nbytes = attention_workspace_bytes(cache, batch.B, T, Hq)
     if workspace is None:

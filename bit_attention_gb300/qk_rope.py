@@ -238,9 +238,21 @@ class _Call:
             _on(self.dev, qo, ko)
             _fp4._own_elements(qo, "out")
             _fp4._own_elements(ko, "out")
+            self.in_place(qo, sqo, ko, sko)
         _fp4._call(lib().sage_rope_fwd, "sage_rope_fwd", self.dev, stream, (qo, ko, table.cos_sin, table.status, *tensors),
                    self.desc, self.q, self.sq, self.k, self.sk, qo.data_ptr(), sqo, ko.data_ptr(), sko)
         return qo, ko
+
+    def in_place(self, qo, sqo, ko, sko):
+        """Refuse results that start where another tensor does, but for each input's
+        own place and strides."""
+        if not qo.numel() or not ko.numel():
+            return
+        qp, kp = qo.data_ptr(), ko.data_ptr()
+        same = lambda a, b: (a.b, a.h, a.n) == (b.b, b.h, b.n)  # noqa: E731
+        if qp == kp or qp == self.k or kp == self.q or (qp == self.q and not same(sqo, self.sq)) or \
+                (kp == self.k and not same(sko, self.sk)):
+            raise SageFp4Error(EINVAL, "out shares memory with q or k other than in place")
 
     def backward(self, gq, gk, table, layout: str, grad_layout: str, stream, tensors):
         import torch
@@ -290,7 +302,8 @@ def forward(q, k, positions, table: RopeTable, q_weight=None, k_weight=None, eps
     are rotated only.  interleaved: pairs (2i, 2i + 1) instead of (i, i + rot/2).
     out_layout: layout of the results (the inputs' by default; "HND" is what
     the attention calls take).  out: (q', k') to write, the inputs themselves
-    among the choices.  Asynchronous; a position outside the table gives zeros
+    among the choices (each in its own place, with its own strides; no other memory
+    is shared).  Asynchronous; a position outside the table gives zeros
     and EINDEX in table.get_status()."""
     call = _Call(q, k, positions, table, q_weight, k_weight, eps, interleaved, layout)
     return call.forward(table, layout if out_layout is None else out_layout, out, stream,

@@ -768,3 +768,22 @@ def test_lengths_next_to_the_largest_int_are_recorded_and_left_out(fmt, nq):
         R.check_attention(b, q, o, lse)
         k, v = KV.read(b.cache, lens, table, 64)
         assert b.cache.get_status() == S.EINDEX and (k[0] == 0).all() and (v[0] == 0).all() and (k[1] != 0).any()
+
+
+def test_outputs_laid_over_inputs_are_refused():
+    b = R.Batch("bf16", 2, 64, 16, [3, 200], [20, 300])
+    q = bf16(b.rng.standard_normal((b.T, 4, 64)))
+    wide = torch.zeros((b.T, 8, 64), dtype=torch.bfloat16, device="cuda")
+    dense = torch.zeros((2, 2, 8, 64), dtype=torch.bfloat16, device="cuda")
+    cu, n, table = b.args()
+    keep = q.clone()
+    for call in (lambda: KV.attention(q, b.cache, cu, n, table, out=q),
+                 lambda: KV.attention(wide[:, ::2], b.cache, cu, n, table, out=wide[:, :4]),
+                 lambda: KV.read(b.cache, n, table, 8, out=(dense, dense))):
+        with pytest.raises(S.SageFp4Error) as e:
+            call()
+        assert e.value.code == S.EINVAL
+    assert torch.equal(q, keep) and (dense == 0).all() and b.cache.get_status() == S.OK
+    wide[:, :4] = q  # side by side in one tensor they are apart
+    KV.attention(wide[:, :4], b.cache, cu, n, table, out=wide[:, 4:])
+    assert torch.equal(wide[:, 4:], KV.attention(q, b.cache, cu, n, table))

@@ -413,3 +413,22 @@ def test_gradients_through_sagebwd_are_those_of_the_calls_by_hand():
     SB.attention(*y, v.detach(), causal=True).backward(do)
     by_hand = Q.backward(y[0].grad, y[1].grad, q, k, p, table, *w, grad_layout="HND")
     assert all(torch.equal(x.grad, g) for x, g in zip(leaves, by_hand))
+
+
+def test_results_laid_over_inputs_other_than_in_place_are_refused():
+    rng, q, k, w = case(18, 2, 9, 4, 4, 64)
+    q, k = q.contiguous(), k.contiguous()
+    table = Q.rope_table(64, 64)
+    p = torch.arange(9, dtype=torch.int32, device="cuda")
+    fresh = [torch.empty_like(x) for x in (q, k)]
+    anew = q.view(2, 4, 9, 64)  # q's memory as [B, H, N, D]
+    keep = [q.clone(), k.clone()]
+    for out, layout in (((k, q), "NHD"), ((fresh[0], fresh[0]), "NHD"), ((k, fresh[1]), "NHD"), ((fresh[0], q), "NHD"),
+                        ((anew, torch.empty_like(anew)), "HND")):
+        with pytest.raises(S.SageFp4Error) as e:
+            Q.forward(q, k, p, table, *w, out=out, out_layout=layout)
+        assert e.value.code == S.EINVAL
+    assert torch.equal(q, keep[0]) and torch.equal(k, keep[1]) and table.get_status() == S.OK
+    ref = Q.forward(q, k, p, table, *w)
+    Q.forward(q, k, p, table, *w, out=(fresh[0], k))  # one of the two in place
+    assert torch.equal(fresh[0], ref[0]) and torch.equal(k, ref[1])
