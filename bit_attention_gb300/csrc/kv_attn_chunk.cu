@@ -32,7 +32,7 @@
 // below says where that is exact and what else is done.  Q's rows are scaled by the power
 // of two that brings their largest magnitude to 2^14 .. 2^15: bf16's eight bits
 // fit while a channel is above 2^-28 of it.  P is rounded to bf16 (2^-8
-// relative) or FP16 (weights of 2^7 at the reference: 2^-12 relative down to
+// relative) or FP16 (weights of 2^7 at the reference: 2^-11 relative down to
 // 2^-21, 2^-32 below); the row sums take the FP32 values.
 #include "kv_attn.cuh"
 #include "umma.cuh"

@@ -32,7 +32,7 @@
 // 2^-10 .. 2688).  Q becomes FP16 after its row is scaled by the power of two
 // that brings its largest magnitude to 2^14 .. 2^15: bf16's eight bits fit
 // while a channel is above 2^-28 of the row's largest.  P is rounded to FP16
-// (the largest weight raised to 2^11 .. 2^15: half a step is 2^-12 relative down
+// (the largest weight raised to 2^11 .. 2^15: half a step is 2^-11 relative down
 // to 2^-25 of it, and 2^-36 of it below) or, for a bf16 cache, to bf16; sums and
 // statistics are FP32.
 #include "kv_attn.cuh"
