@@ -70,8 +70,8 @@ struct Smem {
   static constexpr int kKScale = kScale + 8 * 16;     // [8 tiles][4] K's scale of 32 keys (E4M3), 0: wide
   static constexpr int kBytes = kKScale + 8 * 16;     // [kInfo tiles][2][128] scale bytes of K and V (E4M3, wide rows)
   static constexpr int kInfo = D == 64 ? 8 : 4;       // (a tile's are read before the one three tiles on is written)
-  static constexpr int kMisc = kBytes + kInfo * 256;        // tensor-memory address, abort flag, spread of
-                                                           // V's scales [2], pieces to redo [8 softmax warps]
+  static constexpr int kMisc = kBytes + kInfo * 256;        // tensor-memory address, abort flag, V scales
+                                                           // seen, pieces to redo [8 softmax warps]
   static constexpr int kAlloc = kMisc + 48 + 1024;    // with room to align to 1024
 };
 static_assert(Smem<128>::kAlloc <= 227 * 1024 && Smem<64>::kAlloc <= 227 * 1024, "shared memory");
@@ -227,9 +227,9 @@ struct Scales {
   // a share whose V scales are further apart may leave weights of the least out of
   // the row sum: its rows are done again
   static constexpr int kMostV = 92;
-  static constexpr int kBias = 127 + 7;
+  static constexpr uint32_t kBias = 127 + 7;
   uint32_t top_k, top_v, mine_k, mine_v;  // largest; this lane's factors
-  uint32_t low_v;                         // for kMostV
+  uint32_t seen;                          // V's scales in eights, a bit each
   bool wide;
 
   static __device__ __forceinline__ uint32_t largest(uint32_t v) {
@@ -237,9 +237,15 @@ struct Scales {
     asm volatile("redux.sync.max.u32 %0, %1, 0xffffffff;" : "=r"(r) : "r"(v));
     return r;
   }
+  static __device__ __forceinline__ uint32_t smallest(uint32_t v) {
+    uint32_t r;
+    asm volatile("redux.sync.min.u32 %0, %1, 0xffffffff;" : "=r"(r) : "r"(v));
+    return r;
+  }
   // 2^(7 - d) as an FP16 pair
   static __device__ __forceinline__ uint32_t factor(uint32_t d) {
-    return (d < 22 ? (22u - d) << 10 : d < 32 ? 1u << (31 - d) : 0u) * 0x10001u;
+    const float f = __uint_as_float((kBias - d) << 23);
+    return h2_of(f, f);
   }
   // k, v: the lane's scale bytes, 0 where it has no row
   __device__ __forceinline__ Scales(uint32_t k, uint32_t v) {
@@ -247,12 +253,15 @@ struct Scales {
     const uint32_t least = v < kLeastV ? kLeastV : v;
     top_k = largest(kz ? kZero + 1 : k);
     top_v = largest(least);
-    wide = __any_sync(kAll, (!kz && k + kSpreadK < top_k) || (!vz && least + kSpreadV < top_v));
+    wide = top_k > smallest(kz ? 255u : k) + kSpreadK || top_v > smallest(vz ? 255u : least) + kSpreadV;
     mine_k = kz ? 0u : factor(wide ? 0 : top_k - k);
     mine_v = vz ? 0u : factor(wide ? least - v : top_v - v);
+    seen = 1u << (top_v / 8);
     // (a wide share's weights are summed by themselves: only the sum's own range counts)
-    low_v = wide ? min(255u - largest(v ? 255u - least : 0u) + 126u - kMostV, 255u) : top_v;
+    if (wide) seen |= 1u << (min(smallest(v ? least : 255u) + (126 - kMostV), 255u) / 8);
   }
+  // of a CTA's shares
+  static __device__ __forceinline__ bool apart(uint32_t all) { return all && (31 - __clz(all)) - (__ffs(all) - 1) > kMostV / 8 - 1; }
 };
 
 // 32 bf16 rows to an operand tile by asynchronous 16-byte copies; a missing
@@ -310,7 +319,7 @@ __device__ __noinline__ Row wide_tile(uint32_t tS, uint32_t tO, uint32_t bar_p, 
     for (int e = 0; e < 8; e++) {
       const uint32_t k = (kb[e / 4] >> (8 * (e % 4))) & 255u, w = (vb[e / 4] >> (8 * (e % 4))) & 255u;
       const float f = kf > 0.0f ? kf : k > Scales::kZero ? __uint_as_float((k + 127 - Scales::kBias) << 23) : 0.0f;
-      v[e] = kf > 0.0f ? vx : static_cast<float>(static_cast<int>(max(w, Scales::kLeastV)) - Scales::kBias);
+      v[e] = kf > 0.0f ? vx : static_cast<float>(static_cast<int>(max(w, Scales::kLeastV) - Scales::kBias));
       u[e] = (on >> e) & 1 ? __uint_as_float(r[e]) * (factor * f) : -INFINITY;
     }
   };
@@ -462,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) { return sbase + L::kBar + 8 * i; };
   uint32_t* tslot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
-  uint32_t* spread = reinterpret_cast<uint32_t*>(smem + L::kMisc + 8);  // V's scales: the largest, 255 less the least
+  uint32_t* spread = reinterpret_cast<uint32_t*>(smem + L::kMisc + 8);
   uint32_t* lost = reinterpret_cast<uint32_t*>(smem + L::kMisc + 16);
   uint32_t* mask = reinterpret_cast<uint32_t*>(smem + L::kMask);
   float* vlog = reinterpret_cast<float*>(smem + L::kScale);
@@ -488,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(bar(B_DRAIN), 1);
     *abort = 0;
-    spread[0] = spread[1] = 0;
+    *spread = 0;
     for (int i = 0; i < 8; i++) lost[i] = 0;
     mbar_fence_init();
   }
@@ -770,8 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       cur = next;
     }
     __syncwarp();
-    const bool apart = kScales && static_cast<int>(spread[0] + spread[1]) > 255 + Scales::kMostV;
-    const uint32_t redo = __any_sync(kAll, apart) ? kAll : lost[warp];
+    const uint32_t redo = kScales && __any_sync(kAll, Scales::apart(*spread)) ? kAll : lost[warp];
     if (ok && redo) redo_pieces<kFmt, D>(c, a, work, redo, 128 * m + 32 * (warp & 3));
     tc_fence_before();
   } else if (wg == 2) {
@@ -878,9 +886,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (lane == 0) {
             kscale[4 * (tiles & 7) + w] = x.wide ? 0.0f : __uint_as_float((x.top_k + 127 - Scales::kBias) << 23);
-            vlog[4 * (tiles & 7) + w] = static_cast<float>(static_cast<int>(x.top_v) - Scales::kBias);
-            atomicMax(spread, x.top_v);
-            atomicMax(spread + 1, 255u - x.low_v);
+            vlog[4 * (tiles & 7) + w] = static_cast<float>(static_cast<int>(x.top_v - Scales::kBias));
+            atomicOr(spread, x.seen);
           }
         }
         if (lane == 0) mask[4 * (tiles & 7) + w] = here;
