@@ -19,9 +19,9 @@
 // Bound by that alternation: a pair of tiles takes 2050 cycles of MMA at the
 // tensor cores' rate (2780 measured: S reads both operands from shared memory,
 // at its bandwidth), and the chain of one tile's S, softmax and P V 3200.  A
-// prompt of 8192 tokens, 32 query and 8 key/value heads of 128, bf16: 372 us,
-// 1.48 PFLOP/s, tensor pipe busy 65%; 1121 new tokens over 37000 in E4M3, whose
-// conversion keeps the gather at 3300 .. 3600 cycles a pair: 190 us, 1.17 PFLOP/s.
+// prompt of 8192 tokens, 32 query and 8 key/value heads of 128, bf16: 373 us,
+// 1.47 PFLOP/s, tensor pipe busy 66%; 1121 new tokens over 37000 in E4M3, whose
+// conversion keeps the gather at 3300 .. 3600 cycles a pair: 199 us, 1.12 PFLOP/s.
 //
 // Operand types.  For a bf16 cache both products are bf16.  For the quantized
 // ones they are FP16, into which stored values convert in two instructions a

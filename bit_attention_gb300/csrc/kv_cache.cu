@@ -7,7 +7,8 @@
 // has several rows in flight, of k and of v, and asks for them before the chain
 // of small loads (sequence bounds, length, page) that says where they go.
 // 65536 tokens of 8 heads of 128: bf16 86 us (6.2 TB/s), E4M3 69 (5.9), NVFP4 71
-// (4.9, where converting bounds it); back again 86, 75 and 71.
+// (4.9, where converting bounds it: issue in 80% of cycles); back again 86, 75 and 71
+// (issue in 64% and 70%).
 #include "kv.cuh"
 
 namespace sagefp4 {

@@ -14,7 +14,8 @@
 // the next ones' loads in flight, was slower: 96 registers instead of 64 leave
 // 20 warps an SM.)
 // 16384 tokens of 32 + 8 heads of 128: forward 59 us, 5.8 TB/s; 8192 tokens of 16 +
-// 16 heads: backward 41 us, 4.9 TB/s (a row's two sums through shuffles there).
+// 16 heads: backward 41 us, 4.9 TB/s (128 registers leave it 16 warps an SM, which
+// issue in 54% of cycles).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>

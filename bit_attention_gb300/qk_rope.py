@@ -109,8 +109,9 @@ def rope_table(positions: int, rot: int, base: float = 10000.0, scaling: str | N
     None; "linear": every angle divided by `factor` (position interpolation);
     "yarn": pairs that turn more than 32 times over the `trained` positions
     keep their angle, pairs that turn less than once are divided by `factor`,
-    those between go linearly from one to the other, and cos and sin are
-    multiplied by 0.1 ln(factor) + 1."""
+    those between go linearly (in turns, as the method was published; some programs
+    let the ramp run over the pair's index, which wants a RopeTable of one's own)
+    from one to the other, and cos and sin are multiplied by 0.1 ln(factor) + 1."""
     import torch
     if positions < 1 or not math.isfinite(base) or base <= 0:
         raise SageFp4Error(EINVAL, f"positions {positions}, base {base}")

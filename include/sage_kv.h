@@ -29,7 +29,8 @@
  * cache is attention over exactly these bf16 values, whatever the sizes of the rows
  * around one and whether they are seen (but E4M3 rows below 2^-101 in magnitude may
  * count as zeros; where 32 neighbouring values differ by more than 2^8 calls of many
- * rows take longer).
+ * rows take longer).  Over quantized caches queries enter in FP16, relative to their
+ * row's largest magnitude: exact down to 2^-28 of it.
  *
  * Layout of the buffers (contiguous, 16-byte aligned, k and v alike):
  *   codes  [num_pages][H][page_size][D], [D / 2] bytes for NVFP4;
