@@ -206,9 +206,11 @@ __global__ void __launch_bounds__(256) combine_chunk_kernel(const __grid_constan
     float4 v[kN];
 #pragma unroll
     for (int k = 0; k < kN; k++) v[k] = o[static_cast<size_t>(d0 * kN + k) * kChunkRows];
+    // in two steps each: over E4M3 what a part is relative to counts V's scale, and its
+    // sum makes up for that, so that a factor may be below FP32 where the product is not
     const float mn = fmaxf(m, ml.x), sub = mn == -INFINITY ? 0.0f : mn;
-    const float f0 = ex2_approx(m - sub), f1 = ex2_approx(ml.x - sub);
-    l = l * f0 + ml.y * f1;
+    const float h0 = ex2_approx(0.5f * (m - sub)), h1 = ex2_approx(0.5f * (ml.x - sub)), f0 = h0 * h0, f1 = h1 * h1;
+    l = l * h0 * h0 + ml.y * h1 * h1;
 #pragma unroll
     for (int k = 0; k < kN; k++) {
       acc[k] = float4{acc[k].x * f0, acc[k].y * f0, acc[k].z * f0, acc[k].w * f0};

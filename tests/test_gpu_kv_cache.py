@@ -787,3 +787,26 @@ def test_outputs_laid_over_inputs_are_refused():
     wide[:, :4] = q  # side by side in one tensor they are apart
     KV.attention(wide[:, :4], b.cache, cu, n, table, out=wide[:, 4:])
     assert torch.equal(wide[:, 4:], KV.attention(q, b.cache, cu, n, table))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("q_lens,kv_lens", [([2], [290]), ([140], [290]), ([140], [2900])])
+def test_huge_scores_below_zero_before_others_and_channels_of_zeros(fmt, q_lens, kv_lens):
+    # nothing of the first half of the keys, whose scores are far below 0, is left in
+    # any channel, whatever the first channels hold
+    D, n = 64, kv_lens[0]
+    b = R.Batch(fmt, 1, D, 16, q_lens, kv_lens, seed=33, fill=False)
+    k, v = np.zeros((n, 1, D)), b.rng.standard_normal((n, 1, D))
+    k[:n // 2, 0, 0] = -4.0
+    v[:, :, :16] = 0.0
+    KV.append(b.cache, bf16(k), bf16(v), torch.tensor([0, n], dtype=torch.int32, device="cuda"), b.kv_len, b.block_table)
+    q = np.zeros((b.T, 10, D))
+    q[:, :, 0] = 2.0 ** np.array([10, 20, 24, 28, 31, 33, 36, 50, 80, 100])
+    o = R.f64(KV.attention(bf16(q), b.cache, *b.args()))
+    vd = b.dense("v", 0)[0]
+    for i in range(b.T):
+        seen = vd[n // 2:n - b.T + i + 1]
+        # weights alike but for a rounding each (2^-8), and the result's; FP32 sums of up to 2^11 terms
+        tol = (2.0 ** -8 * 1.01 + 2.0 ** -13) * (np.abs(seen).mean(0) + np.abs(seen.mean(0)))
+        assert (np.abs(o[i] - seen.mean(0)) <= tol).all(), i
+    assert b.cache.get_status() == S.OK

@@ -154,6 +154,18 @@ def test_stretches_of_mixed_and_of_small_values(D, lens, high, low):
     check(b, bf16(rng.standard_normal((b.T, 4, D))), lens[0][0] > 4)
 
 
+@pytest.mark.parametrize("lens", [([2], [20000]), ([140], [20000])])
+@pytest.mark.parametrize("halves", [(90, -60), (-60, 90), (0, -95)])
+def test_halves_of_a_long_sequence_of_very_different_sizes(lens, halves):
+    # shares that see one size alone and are joined: the weights of both count
+    rng = np.random.default_rng(7)
+    n = lens[1][0]
+    k, v = rng.standard_normal((2, n, 1, 64))
+    v *= 2.0 ** np.where(np.arange(n) < n // 2, *map(float, halves))[:, None, None]
+    b = filled(k, v, *lens, 1, 64, page=64)
+    check(b, bf16(rng.standard_normal((b.T, 4, 64))), lens[0][0] > 4)
+
+
 @pytest.mark.parametrize("lens", [FEW, MANY])
 def test_rows_of_zeros_and_next_to_zero(lens):
     # magnitudes down to bf16's smallest, where the scale's byte stops at its least
