@@ -280,7 +280,9 @@ __device__ __forceinline__ void copy_rows(uint32_t tile, int base, const uint8_t
 }
 
 // ------------------------------------------------------------------ softmax
-template <int D>
+// kWipe: an infinite O becomes 0 by a factor of 0.  (FP16 weights need it not: what an
+// infinite one leaves in every channel of O shows later.)
+template <int D, bool kWipe = false>
 __device__ __forceinline__ void rescale_o(uint32_t tO, float alpha) {
 #pragma unroll 1
   for (int j = 0; j < D; j += 8) {
@@ -288,7 +290,7 @@ __device__ __forceinline__ void rescale_o(uint32_t tO, float alpha) {
     tmem_ld8(tO + j, o);
     tmem_wait_ld();
 #pragma unroll
-    for (int e = 0; e < 8; e++) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+    for (int e = 0; e < 8; e++) o[e] = !kWipe || alpha > 0.0f ? __float_as_uint(__uint_as_float(o[e]) * alpha) : 0u;
     tmem_st8(tO + j, o);
   }
   tmem_wait_st();
@@ -669,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ref = to;
           const bool some = __any_sync(kAll, l > 0.0f);  // else O holds nothing, or nothing yet
           l *= alpha;
-          if (some) rescale_o<D>(tO, alpha);
+          if (some) rescale_o<D, !kHalf>(tO, alpha);
         }
         const float sub = (ref == -INFINITY ? 0.0f : ref) - kRaise;
 #pragma unroll
