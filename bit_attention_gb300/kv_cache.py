@@ -286,7 +286,10 @@ def attention(q, cache: PagedCache, cu_q, kv_len, block_table, causal: bool = Tr
     the cache.  return_lse: also the natural-log log-sum-exp, float32
     [T, Hq] (-inf for a row that sees nothing).  workspace: uint8 tensor of
     attention_workspace_bytes (a temporary one by default); calls sharing one
-    must be ordered."""
+    must be ordered.
+
+    One kernel serves a call, by its average of new tokens a sequence: single
+    tokens and long chunks are faster in a call each."""
     import torch
     batch = _batch(cache, cu_q, kv_len, block_table)
     T, Hq, qr = _rows(q, cache, "q")
